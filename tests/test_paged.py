@@ -370,6 +370,27 @@ def test_paged_attn_bad_pages_and_lengths_are_reported(cuda_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bad", [-1, -2, -3, "n_pages", (1 << 31) - 1, -(1 << 31)])
+@pytest.mark.parametrize("page,window,n_sink", [(16, 0, 0), (64, 150, 20), (128, 0, 0)])
+def test_paged_attn_needed_page_outside_the_pool_reads_as_zeros(cuda_lib, bad, page, window, n_sink):
+    """Whatever the id: the status is set, and the sequence's rows are those over
+    zeros in the page's place (which sees keys 128 .. 128 + page - 1)."""
+    api = cuda_lib
+    b = Batch([(300, 2), (200, 1), (290, 40)], 8, 2, page, seed=page)
+    for i in (0, 2):
+        b.table[i][128 // page] = b.n_pages if bad == "n_pages" else bad
+        b.k[i][128:128 + page] = 0
+        b.v[i][128:128 + page] = 0
+    b.table_t = i32(b.table)
+    p, (O, lse) = b.params(api, window, n_sink), b.out()
+    ws = api.alloc_paged_workspace(p)
+    for _ in range(2):
+        api.paged_attn(p, b.Q, b.K, b.V, b.table_t, b.cu_t, b.len_t, O, lse, ws)
+        assert api.get_status() == api.STATUS_BAD_PAGE
+        b.check(O, lse, window, n_sink)
+
+
+@pytest.mark.gpu
 def test_paged_attn_rows_past_n_tokens_are_cut(cuda_lib):
     """Offsets that pass n_tokens: the rows there are keep their positions."""
     api = cuda_lib
