@@ -444,8 +444,11 @@ int infllmv2_paged_append(const infllmv2_paged_params* p, const int32_t* slots, 
  * Only pages with a visible key are read: pages that left the window (and hold
  * no sink) may have been given to others.  Anything may lie in a sequence's
  * last page behind its last token.  An id outside the pool that is needed sets
- * INFLLMV2_STATUS_BAD_PAGE; its keys and values are read as zeros.  Lengths
- * outside their arrays are cut to them.
+ * INFLLMV2_STATUS_BAD_PAGE; its keys and values are read as zeros.  A row at a
+ * position past the table (t >= max_pages * page_size: a token that found no
+ * slot) gets O = 0 and lse = -inf; the sequence's other rows keep theirs.
+ * Negative lengths count as 0, lengths past 2^30 as 2^30, and rows past n_tokens
+ * are cut.
  */
 int infllmv2_paged_attn(const infllmv2_paged_params* p, const void* Q, int64_t q_stride,
                         const void* K_pages, const void* V_pages, const int32_t* block_table,

@@ -405,6 +405,31 @@ def test_paged_attn_rows_past_n_tokens_are_cut(cuda_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("past,window,n_sink", [(1, 0, 0), (6, 0, 0), (6, 20, 3), (30, 0, 0), (200, 9, 0),
+                                                (1 << 29, 0, 0)])
+def test_paged_attn_tokens_past_the_table_leave_the_others_their_positions(cuda_lib, past, window,
+                                                                           n_sink):
+    """A sequence whose new tokens outgrow its table row: rows that have a place
+    stand where they stand, the others get O = 0 and lse = -inf."""
+    api, page = cuda_lib, 16
+    b = Batch([(64, 30), (40, 3), (64, 1), (100, 100)], 8, 2, page, seed=12, pad=2)
+    b.width, b.table = 4, [r[:4] for r in b.table]      # room for 64 keys
+    b.table_t = i32(b.table)
+    b.len_t = i32([64 + past, 40, 64, 100])
+    b.k[3], b.v[3] = b.k[3][:64], b.v[3][:64]
+    O, lse = b.run(api, window, n_sink)
+    o, ls, q = f64(O), f64(lse), f64(b.Q)
+    pos = [np.arange(64 + past - 30, 64 + past), np.arange(37, 40), [63], np.arange(100)]
+    for i, t in enumerate(pos):
+        t, rows = np.asarray(t), np.arange(b.cu[i], b.cu[i + 1])
+        has = t < 64
+        ref = wo.attention(q[rows[has]], f64(b.k[i]), f64(b.v[i]), t[has], window, n_sink)
+        check(o[rows[has]], ls[rows[has]], ref, 64)
+        assert (o[rows[~has]] == 0).all() and np.isneginf(ls[rows[~has]]).all()
+    assert (o[b.cu[-1]:] == 7).all() and (ls[b.cu[-1]:] == 7).all()
+
+
+@pytest.mark.gpu
 def test_paged_attn_replayed_with_other_lengths_and_two_workspaces(cuda_lib):
     """One captured call serves changing lengths; two calls in flight on two
     streams, a workspace each, give what they give alone."""

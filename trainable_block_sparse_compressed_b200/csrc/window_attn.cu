@@ -121,6 +121,7 @@ struct FwdItem {
 
 struct SeqLens {
   int row0, n_q, t0;  // first row, new tokens, position of the first
+  int n_past;         // rows behind them whose positions lie past the table
 };
 
 // Lengths of sequence i with every value brought into range: nothing that the
@@ -129,13 +130,13 @@ __device__ __forceinline__ SeqLens seq_lens(const FwdArgs& a, int i) {
   SeqLens s;
   const int r0 = __ldg(a.cu_q + i), r1 = __ldg(a.cu_q + i + 1);
   const int c0 = max(0, min(r0, a.n_tokens)), c1 = max(0, min(r1, a.n_tokens));
-  const long long cap = static_cast<long long>(a.max_pages) * a.page;
-  const int k = static_cast<int>(max(0ll, min(static_cast<long long>(__ldg(a.seqlens + i)), cap)));
-  s.row0 = c0;
-  s.n_q = max(0, c1 - c0);
-  // (rows past n_tokens are cut, the others keep their positions)
+  // (rows that are cut, at either end, leave the others their positions)
   const long long len = min(max(static_cast<long long>(r1) - r0, 0ll), 1ll << 28);
-  s.t0 = k - static_cast<int>(len);
+  s.t0 = max(0, min(__ldg(a.seqlens + i), 1 << 30)) - static_cast<int>(len);
+  s.row0 = c0;
+  const int rows = max(0, c1 - c0);
+  s.n_q = max(0, min(rows, a.max_pages * a.page - s.t0));
+  s.n_past = rows - s.n_q;
   return s;
 }
 
@@ -267,6 +268,17 @@ __device__ long long head_units(const FwdArgs& a, const SeqLens& s) {
          key_tiles(a.vis, s.t0 + last * IT, s.t0 + s.n_q - 1).n + kItemUnits;
 }
 
+// The rows of tokens that found no place in the table: O = 0, lse = -inf.  One
+// thread of each CTA calls it, which takes every gridDim.x-th row.
+__device__ __forceinline__ void no_place(const FwdArgs& a, const SeqLens& s) {
+  for (int r = s.n_q + blockIdx.x; r < s.n_q + s.n_past; r += gridDim.x) {
+    const int64_t at = (static_cast<int64_t>(s.row0) + r) * a.Hq;
+    uint4* o = reinterpret_cast<uint4*>(a.O + at * kHeadDim);
+    for (int c = 0; c < a.Hq * (kHeadDim / 8); ++c) o[c] = make_uint4(0, 0, 0, 0);
+    for (int h = 0; h < a.Hq; ++h) a.lse[at + h] = -INFINITY;
+  }
+}
+
 // The paged schedule: the units of all items in a row (sequence, head, query
 // tiles) are cut into equal ranges, one per CTA; an item cut by a range's end
 // gets partial results that the merge kernel joins.  Every CTA derives its own
@@ -279,9 +291,11 @@ __device__ void paged_schedule(const FwdArgs& a, FwdSmem& sm) {
   for (int i0 = 0; i0 < a.n_seqs; i0 += kThreads) {
     const int i = i0 + threadIdx.x;
     if (i < a.n_seqs) {
-      const long long u = a.Hkv * head_units<IT>(a, seq_lens(a, i));
+      const SeqLens s = seq_lens(a, i);
+      const long long u = a.Hkv * head_units<IT>(a, s);
       if (i0 == 0) mine0 = u;
       total += u;
+      if (s.n_past > 0) no_place(a, s);
     }
   }
 #pragma unroll
