@@ -387,7 +387,8 @@ typedef struct infllmv2_paged_params {
  * Block tables and slot maps of one step, built on the GPU from the requests'
  * lengths.  With P = page_size, kv_i = kv_lens[i] cached and q_i = q_lens[i]
  * new tokens (a length counts as one from 0 to 2^28):
- *   have_i = ceil(kv_i / P), want_i = ceil((kv_i + q_i) / P),
+ *   have_i = ceil(kv_i / P), want_i = ceil((kv_i + q_i) / P), neither more than
+ *     max_pages (no page is taken for a column that the table lacks),
  *   first_i = sum_{j<i} (want_j - have_j),
  *   block_table[i, c] = free_pages[*free_count - 1 - first_i - (c - have_i)] for
  *     have_i <= c < want_i (the free list is a stack; other entries stay);

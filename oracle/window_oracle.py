@@ -86,7 +86,8 @@ def backward(q, K, V, dO, window, n_sink, scale=None):
 
 def paged_tables(kv_lens, q_lens, free_pages, table, page, n_tokens):
     """Block tables and slot maps, request by request: pages are popped off
-    the end of free_pages; -1 where there is none.  Returns (table, cu_q,
+    the end of free_pages, none for a column that the table lacks; -1 where
+    there is none.  Returns (table, cu_q,
     seqlens, slots, positions, free_left, taken_all)."""
     table = [list(r) for r in table]
     stack = list(free_pages)
@@ -94,14 +95,10 @@ def paged_tables(kv_lens, q_lens, free_pages, table, page, n_tokens):
     slots, positions = [-1] * n_tokens, [-1] * n_tokens
     for i, (kv, q) in enumerate(zip(kv_lens, q_lens)):
         kv, q = max(kv, 0), max(q, 0)
-        new = {}
-        for c in range(-(-kv // page), -(-(kv + q) // page)):
-            new[c] = stack.pop() if stack else -1
-            fine = fine and new[c] != -1
-            if c < len(table[i]):
-                table[i][c] = new[c]
-            else:
-                fine = False
+        for c in range(-(-kv // page), min(-(-(kv + q) // page), len(table[i]))):
+            table[i][c] = stack.pop() if stack else -1
+            fine = fine and table[i][c] != -1
+        fine = fine and not (q > 0 and kv + q > len(table[i]) * page)
         for j in range(q):
             r, t = cu[-1] + j, kv + j
             if r >= n_tokens:

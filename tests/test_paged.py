@@ -91,6 +91,27 @@ def test_paged_tables_too_long_and_negative(cuda_lib):
 
 
 @pytest.mark.gpu
+def test_paged_tables_take_no_page_for_a_column_that_the_table_lacks(cuda_lib):
+    """Two of four requests outgrow their rows of three columns: the free list
+    loses the pages that were entered and no others, and the requests behind
+    them get theirs."""
+    api, page = cuda_lib, 16
+    kv, q = [40, 0, 60, 10], [30, 100, 1, 20]
+    table = [[0, 1, 2], [-1, -1, -1], [3, 4, 5], [6, -1, -1]]
+    free = [7, 8, 9, 10, 11]
+    got = run_tables(api, kv, q, free, table, page, 151, 12)
+    # request 1 takes three pages, request 3 one
+    assert got[0] == [[0, 1, 2], [11, 10, 9], [3, 4, 5], [6, 8, -1]] and got[5] == 1
+    *ref, fine = wo.paged_tables(kv, q, free, table, page, 151)
+    assert not fine and got == tuple(ref)
+    assert api.get_status() == api.STATUS_SEQ_FULL
+    # a request already past its row takes none either
+    got = run_tables(api, [70], [5], [1, 2], [[0, 3, 4]], page, 5, 5)
+    assert got == ([[0, 3, 4]], [0, 5], [75], [-1] * 5, [70, 71, 72, 73, 74], 2)
+    assert api.get_status() == api.STATUS_SEQ_FULL
+
+
+@pytest.mark.gpu
 def test_paged_tables_nonsense_lengths_stay_inside(cuda_lib):
     """Lengths whose sums pass 32 bits: ascending offsets, every slot and entry
     inside, the status set."""

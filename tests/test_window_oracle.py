@@ -67,3 +67,12 @@ def test_tables_by_hand():
     assert cu == [0, 3, 4, 4] and lens == [6, 1, 4]
     assert slots == [7 * 4 + 3, 12 * 4, 12 * 4 + 1, 11 * 4, -1, -1]
     assert pos == [3, 4, 5, 0, -1, -1]
+
+
+def test_tables_take_no_page_for_a_column_that_the_table_lacks():
+    # pages of 4, two columns: request 0 takes one page for 9 tokens past its
+    # first 3, request 1 gets the next
+    table, cu, lens, slots, pos, left, fine = wo.paged_tables(
+        [3, 0], [9, 1], [10, 11, 12], [[7, -1], [-1, -1]], 4, 10)
+    assert table == [[7, 12], [11, -1]] and left == 1 and not fine
+    assert slots == [31, 48, 49, 50, 51, -1, -1, -1, -1, 44] and lens == [12, 1]

@@ -6,7 +6,7 @@
 // tokens of 8 kv heads (67 MB) 12 us from HBM (5.5 TB/s).
 //
 // Tables.  For request i with kv_i cached and q_i new tokens, pages of P:
-//   have_i = ceil(kv_i / P), want_i = ceil((kv_i + q_i) / P),
+//   have_i = ceil(kv_i / P), want_i = ceil((kv_i + q_i) / P), neither more than max_pages,
 //   cu_q = exclusive sum of q,  first_i = sum_{j<i} (want_j - have_j),
 //   table[i, c] = free_pages[free_count - 1 - first_i - (c - have_i)],  have_i <= c < want_i,
 //   token j of i: position kv_i + j, slot = table[i, position / P] * P + position % P.
@@ -52,13 +52,16 @@ __global__ void __launch_bounds__(kTblThreads) tables_kernel(const TblArgs a, De
   const int P1 = (1 << a.page_shift) - 1;
   const int free_count = max(0, __ldg(a.free_count));
   long long rows = 0, pages = 0;  // of the requests before the strip
+  bool too_long = false;          // a token found no column, or no row
   for (int i0 = 0; i0 < a.n_seqs; i0 += kTblThreads) {
     const int i = i0 + threadIdx.x;
     int k = 0, q = 0, need = 0;
     if (i < a.n_seqs) {
       k = max(0, min(a.kv_lens[i], kMaxLen));
       q = max(0, min(a.q_lens[i], kMaxLen));
-      need = ((k + q + P1) >> a.page_shift) - ((k + P1) >> a.page_shift);
+      need = min((k + q + P1) >> a.page_shift, a.max_pages) -
+             min((k + P1) >> a.page_shift, a.max_pages);
+      too_long = too_long || (q > 0 && k + q > a.max_pages << a.page_shift);
     }
     long long x = q, y = need;
 #pragma unroll
@@ -116,15 +119,12 @@ __global__ void __launch_bounds__(kTblThreads) tables_kernel(const TblArgs a, De
     }
     return lo;
   };
-  bool too_long = false;
   for (int64_t e64 = me; e64 < n_new; e64 += n_thr) {
     const int e = static_cast<int>(e64), i = find(first, e);
     const int k = e - first[i];
     const int c = ((kv[i] + P1) >> a.page_shift) + k;
-    if (c >= 0 && c < a.max_pages)
+    if (INFLLMV2_CHECK(ctx.status, c >= 0 && c < a.max_pages))
       a.table[static_cast<int64_t>(i) * a.max_pages + c] = new_page(i, k);
-    else
-      too_long = true;
   }
   // slots and positions, four rows a thread: one search, and a page looked up
   // again only where the request or the page changes; rows behind the last
@@ -146,9 +146,7 @@ __global__ void __launch_bounds__(kTblThreads) tables_kernel(const TblArgs a, De
         c_last = c;
         const int have = (kv[i] + P1) >> a.page_shift;
         page = -1;
-        if (c < 0 || c >= a.max_pages)
-          too_long = too_long || r < a.n_tokens;
-        else
+        if (c < a.max_pages)
           page = c >= have ? new_page(i, c - have)
                            : a.table[static_cast<int64_t>(i) * a.max_pages + c];
       }
