@@ -68,7 +68,8 @@ extern "C" {
                                                the new tokens n_tokens */
 #define INFLLMV2_STATUS_CHECK          0x4  /* bounds-checked build only: an index check failed
                                                and its access was skipped */
-#define INFLLMV2_STATUS_NO_PAGE        0x8  /* paged_tables: the free list ran out */
+#define INFLLMV2_STATUS_NO_PAGE        0x8  /* paged_tables: the free list ran out, or a new token's
+                                               entry of the table is no page of the pool */
 #define INFLLMV2_STATUS_BAD_PAGE      0x10  /* paged_attn: a page id outside the pool was needed */
 
 /* The method's knobs.  Source of each: the sequence-length switch and the
@@ -398,7 +399,10 @@ typedef struct infllmv2_paged_params {
  *   rows behind the last token: slots = positions = -1;
  *   *free_left = *free_count - (pages taken).
  * Where the free list runs out the entry and its slots are -1 and
- * INFLLMV2_STATUS_NO_PAGE is set; tokens that outgrow max_pages get slot -1,
+ * INFLLMV2_STATUS_NO_PAGE is set.  (A later call that counts those tokens as
+ * cached holds the entry for taken: it stays -1, and every new token that falls
+ * there gets slot -1 and sets the status again, until the caller enters a page
+ * or gives kv_lens without those tokens.)  Tokens that outgrow max_pages get slot -1,
  * tokens past n_tokens get no row, and INFLLMV2_STATUS_SEQ_FULL is set.
  *   kv_lens, q_lens [n_seqs], free_pages [*free_count], free_count [1] int32 (in);
  *   block_table [n_seqs, max_pages] int32 (in/out); cu_q [n_seqs + 1],

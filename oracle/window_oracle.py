@@ -108,6 +108,8 @@ def paged_tables(kv_lens, q_lens, free_pages, table, page, n_tokens):
             p = table[i][t // page] if t // page < len(table[i]) else -1
             if p >= 0:
                 slots[r] = p * page + t % page
+            else:
+                fine = False
         cu.append(cu[-1] + q)
         seqlens.append(kv + q)
     return table, cu, seqlens, slots, positions, len(stack), fine

@@ -112,6 +112,31 @@ def test_paged_tables_take_no_page_for_a_column_that_the_table_lacks(cuda_lib):
 
 
 @pytest.mark.gpu
+def test_paged_tables_replayed_after_a_shortage_keep_reporting_it(cuda_lib):
+    """Lengths in place, the list short by a page in the first step: the steps
+    after it find the entry at -1 and say so, until a page is entered."""
+    import torch
+    api, page = cuda_lib, 16
+    p = api.make_paged_params(2, 4, 6, page, n_tokens=4)
+    lens, q, table = i32([15, 31]), i32([2, 2]), i32([[0, -1, -1, -1], [1, 2, -1, -1]])
+    free, count = i32([3]), i32([1])
+    cu, slots, pos = i32([0] * 3), i32([0] * 4), i32([0] * 4)
+
+    def step():
+        api.paged_tables(p, lens, q, free, count, table, cu, lens, slots, pos, count)
+        return api.get_status(), slots.tolist()
+
+    assert step() == (api.STATUS_NO_PAGE, [15, 48, 47, -1])
+    assert step() == (api.STATUS_NO_PAGE, [49, 50, -1, -1])
+    table[1, 2] = 4
+    assert step() == (0, [51, 52, 67, 68])
+    table[1, 2] = 6      # not a page of the pool
+    assert step() == (api.STATUS_NO_PAGE, [53, 54, -1, -1])
+    torch.cuda.synchronize()
+    assert count.item() == 0 and lens.tolist() == [23, 39]
+
+
+@pytest.mark.gpu
 def test_paged_tables_nonsense_lengths_stay_inside(cuda_lib):
     """Lengths whose sums pass 32 bits: ascending offsets, every slot and entry
     inside, the status set."""

@@ -110,7 +110,6 @@ __global__ void __launch_bounds__(kTblThreads) tables_kernel(const TblArgs a, De
   }
   if (me == 0) a.free_left[0] = max(0, free_count - n_new);
   // new table entries: entry e of all requests' new pages in a row
-  const bool short_of = n_new > free_count;
   auto find = [&](const int32_t* v, int e) -> int {  // last i with v[i] <= e
     int lo = 0, hi = a.n_seqs - 1;
     while (lo < hi) {
@@ -128,7 +127,9 @@ __global__ void __launch_bounds__(kTblThreads) tables_kernel(const TblArgs a, De
   }
   // slots and positions, four rows a thread: one search, and a page looked up
   // again only where the request or the page changes; rows behind the last
-  // token get -1
+  // token get -1.  A token whose column holds no page of the pool is reported: the
+  // list ran out now, or in an earlier step that left the entry at -1.
+  bool no_page = me == 0 && n_new > free_count;
   const bool wide = ((reinterpret_cast<uintptr_t>(a.slots) |
                       reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
   for (int64_t r0 = 4 * static_cast<int64_t>(me); r0 < a.n_tokens; r0 += 4 * static_cast<int64_t>(n_thr)) {
@@ -150,7 +151,10 @@ __global__ void __launch_bounds__(kTblThreads) tables_kernel(const TblArgs a, De
           page = c >= have ? new_page(i, c - have)
                            : a.table[static_cast<int64_t>(i) * a.max_pages + c];
       }
-      if (page >= 0 && page < a.n_pages) slot[x] = (page << a.page_shift) + (pos[x] & P1);
+      if (page >= 0 && page < a.n_pages)
+        slot[x] = (page << a.page_shift) + (pos[x] & P1);
+      else if (c < a.max_pages && r < a.n_tokens)
+        no_page = true;
     }
     if (wide && r0 + 4 <= a.n_tokens) {
       *reinterpret_cast<int4*>(a.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(kTblThreads) tables_kernel(const TblArgs a, De
         if (r0 + x < a.n_tokens) a.slots[r0 + x] = slot[x], a.positions[r0 + x] = pos[x];
     }
   }
-  if (me == 0 && short_of) report_status(ctx.status, INFLLMV2_STATUS_NO_PAGE);
+  if (no_page) report_status(ctx.status, INFLLMV2_STATUS_NO_PAGE);
   if (too_long || (me == 0 && n_rows > a.n_tokens)) report_status(ctx.status, INFLLMV2_STATUS_SEQ_FULL);
 }
 
