@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (ok && walk.next(item)) {
       if (!v_role) {
-        if (ik > 0 && !(ok = guarded_wait(&sm.q_empty, (ik - 1) & 1, ctx, abort_flag))) break;
+        if (ik > 0 && !(ok = warp_wait(&sm.q_empty, (ik - 1) & 1, ctx, abort_flag))) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&sm.q_full, (1 + item.pair) * kTileBytes);
           for (int x = 0; x <= item.pair; ++x)
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = item.k0; i < item.k1; ++i, ++n) {
         const int id = next_id;
         if (PAGED) next_id = page_id(i + 1);
-        if (n >= stages && !(ok = guarded_wait(&empty[st], ph ^ 1, ctx, abort_flag))) break;
+        if (n >= stages && !(ok = warp_wait(&empty[st], ph ^ 1, ctx, abort_flag))) break;
         uint8_t* dst = ring + st * kTileBytes;
         if (PAGED) {
           const bool need = id != kNoKey;
@@ -495,7 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ik = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return guarded_wait(bar, parity & 1, ctx, abort_flag);
+      return PAGED ? warp_wait(bar, parity & 1, ctx, abort_flag)
+                   : warp_poll(bar, parity & 1, ctx, abort_flag);
     };
     for (; ok && walk.next(item); ++ik) {
       const uint32_t step = item.pair ? 1 : 2;

@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 0;  // query tiles before this item
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t phase) {
-        return guarded_wait(bar, phase & 1, ctx, abort_flag);
+        return warp_wait(bar, phase & 1, ctx, abort_flag);
       };
       if (warp == 2) {
         auto issue_s = [&](uint32_t j) -> bool {
@@ -478,8 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long n = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, long long phase) {
-      return __all_sync(0xffffffffu,
-                        guarded_wait(bar, static_cast<uint32_t>(phase & 1), ctx, abort_flag));
+      return warp_wait(bar, static_cast<uint32_t>(phase & 1), ctx, abort_flag);
     };
     for (int ik = 0; ok && walk.next(it); ++ik) {
       const int k0 = it.kt * kKeyTile, key = k0 + key_r;
@@ -774,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 0;  // key tiles before this item
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t phase) {
-        return guarded_wait(bar, phase & 1, ctx, abort_flag);
+        return warp_wait(bar, phase & 1, ctx, abort_flag);
       };
       if (warp == 2) {
         auto issue_s = [&](uint32_t j) -> bool {
@@ -839,8 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ik = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, long long phase) {
-      return __all_sync(0xffffffffu,
-                        guarded_wait(bar, static_cast<uint32_t>(phase & 1), ctx, abort_flag));
+      return warp_wait(bar, static_cast<uint32_t>(phase & 1), ctx, abort_flag);
     };
     for (long long k = blockIdx.x; ok && k < n_items; k += gridDim.x, ++ik) {
       const DqItem it = dq_item<G>(a, k);
