@@ -534,7 +534,8 @@ int infllmv2_get_status(void* stream, int32_t* status_out);
 
 /*
  * Time limit, in nanoseconds, of every device-side bounded wait (mbarrier
- * polls; default 2e9 = 2 s).  A wait that runs out sets
+ * polls; default 2e9 = 2 s; less than 1e6 = 1 ms counts as 1 ms, since a kernel
+ * that gives up still waits for its own copies in flight).  A wait that runs out sets
  * INFLLMV2_STATUS_TIMEOUT, abandons its loop and the kernel returns after
  * releasing its tensor memory.  Takes effect for calls enqueued afterwards.
  */

@@ -48,3 +48,28 @@ def test_the_reading_tells_the_forms_apart():
     assert lone_decisions("if (w) { if (lane == 0) { for (;;) { ok = guarded_wait(b); } } }") == []
     assert lone_decisions("ok = __all_sync(m, ok && guarded_wait(b));") == []
     assert lone_decisions("if (lane == 0) { x(); } ok = guarded_wait(b);") != []
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ns", [0, -5, 1, 999_999])
+def test_no_wait_limit_is_shorter_than_copies_in_flight_take(cuda_lib, ns):
+    """The limit holds for a kernel's own copies too, which it waits for before
+    it returns its shared memory: a limit below 1 ms counts as 1 ms, and real
+    work does not run into it."""
+    import torch
+    from test_window_attn import make, run
+    api = cuda_lib
+    Q, K, V = make(1, 600, 8, 2, seed=1)
+    want = run(api, Q, K, V, 100, 4)
+    api.set_wait_limit(ns)
+    try:
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        api.selftest_timeout()
+        b.record()
+        assert api.get_status() == api.STATUS_TIMEOUT
+        assert a.elapsed_time(b) >= 0.99
+        got = run(api, Q, K, V, 100, 4)
+    finally:
+        api.set_wait_limit(2_000_000_000)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))

@@ -18,6 +18,10 @@ __device__ int g_status_word;
 namespace {
 
 std::atomic<uint64_t> g_wait_ns{2000000000ull};  // 2 s
+// A kernel that gives up waits, with the same limit, for its own copies and
+// products in flight before it returns its shared and tensor memory: no limit
+// may be shorter than those take (microseconds).
+constexpr int64_t kMinWaitNs = 1000000;
 
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
@@ -272,7 +276,7 @@ const char* infllmv2_strerror(int code) {
 }
 
 void infllmv2_set_wait_limit(int64_t ns) {
-  g_wait_ns.store(ns < 0 ? 0ull : static_cast<uint64_t>(ns));
+  g_wait_ns.store(ns < kMinWaitNs ? kMinWaitNs : static_cast<uint64_t>(ns));
 }
 
 size_t infllmv2_workspace_bytes(const infllmv2_params* p, int32_t op) {
