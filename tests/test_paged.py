@@ -188,6 +188,53 @@ def test_paged_tables_replayed_in_place(cuda_lib):
     assert api.get_status() == 0
 
 
+REFUSED_LAUNCH = """
+import torch
+from trainable_block_sparse_compressed_b200 import infllmv2 as api
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+p = api.make_paged_params(1, 2, 4, 16, n_tokens=3)
+args = [i32(0), i32(3), i32(0, 1, 2, 3), i32(4), i32(-1, -1).view(1, 2), i32(0, 0), i32(0),
+        i32(0, 0, 0), i32(0, 0, 0), i32(0)]
+K = torch.zeros(4, 16, 1, 128, dtype=torch.bfloat16, device="cuda")
+rows = torch.ones(3, 1, 128, dtype=torch.bfloat16, device="cuda")
+slots = i32(0, 1, 2)
+torch.cuda.synchronize()
+side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+codes = []
+with torch.cuda.stream(side):
+    graph.capture_begin()
+    try:
+        side.synchronize()          # not allowed in a capture, which it ends
+    except RuntimeError:
+        pass
+    try:
+        api.paged_tables(p, *args)
+    except api.InfLLMV2Error as e:
+        codes.append(e.code)
+    try:
+        graph.capture_end()
+    except RuntimeError:
+        pass
+api.paged_append(p, slots, rows, rows, K, K.clone())
+torch.cuda.synchronize()
+assert codes == [api.ERR_CUDA] and float(K.sum()) == 3 * 128
+print("fine")
+"""
+
+
+@pytest.mark.gpu
+def test_a_refused_launch_fails_its_own_call_alone(cuda_lib):
+    """In a process of its own: a capture that was broken off refuses the
+    tables' launch; the call after it is not told of that."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", REFUSED_LAUNCH], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout[-1000:] + r.stderr[-2000:]
+
+
 # ---------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------

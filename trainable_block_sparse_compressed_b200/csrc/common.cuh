@@ -111,6 +111,14 @@ inline int set_smem_limit(F* func, size_t bytes, std::atomic<uint64_t>& done) {
   return INFLLMV2_OK;
 }
 
+// The code of a launch; a failed one leaves no error behind for the next call's
+// cudaGetLastError().
+inline int launched(cudaError_t e) {
+  if (e == cudaSuccess) return INFLLMV2_OK;
+  cudaGetLastError();
+  return INFLLMV2_ERR_CUDA;
+}
+
 // Tensor maps (tma.cpp).
 int make_tmap_bf16_4d(CUtensorMap* map, const void* base, const uint64_t dims[4],
                       const uint64_t strides_bytes[3], const uint32_t box[4]);

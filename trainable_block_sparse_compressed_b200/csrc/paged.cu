@@ -231,8 +231,7 @@ int launch_paged_tables(const infllmv2_paged_params& p, const int32_t* kv_lens,
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tables_kernel, a, ctx) == cudaSuccess ? INFLLMV2_OK
-                                                                       : INFLLMV2_ERR_CUDA;
+  return launched(cudaLaunchKernelEx(&cfg, tables_kernel, a, ctx));
 }
 
 int launch_paged_append(const infllmv2_paged_params& p, const int32_t* slots, const void* k_new,

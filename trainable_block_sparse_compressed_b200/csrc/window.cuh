@@ -122,9 +122,7 @@ int launch_waiting(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cu
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...) == cudaSuccess
-             ? INFLLMV2_OK
-             : INFLLMV2_ERR_CUDA;
+  return launched(cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...));
 }
 
 // Bits 0 .. n-1 of a 32-bit word.
