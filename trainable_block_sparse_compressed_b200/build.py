@@ -94,7 +94,14 @@ def build_calls() -> str:
 
 
 def build(ptxas_verbose: bool = False, checks: bool = False) -> str:
+    """Builds the library, then the Python module, whose failure (no headers of
+    Python or torch, say) leaves the library built."""
+    lib = build_library(ptxas_verbose, checks)
     build_calls()
+    return lib
+
+
+def build_library(ptxas_verbose: bool = False, checks: bool = False) -> str:
     lib = LIB_CHECKS if checks else LIB
     os.makedirs(os.path.join(BUILD, "checks") if checks else BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
