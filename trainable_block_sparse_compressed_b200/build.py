@@ -15,7 +15,8 @@ variable INFLLMV2_LIB names it.
 
 ``csrc/calls.cpp``, the Python module that checks and passes tensors for the
 calls whose host time counts, becomes ``_calls.so`` (g++, torch's headers); it
-calls whichever of the two libraries is loaded.
+calls whichever of the two libraries is loaded.  It holds to the torch and the
+Python that it was built with, and is rebuilt for others.
 """
 from __future__ import annotations
 
@@ -35,6 +36,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libinfllmv2.so")
 LIB_CHECKS = os.path.join(PKG, "libinfllmv2_checks.so")
 CALLS = os.path.join(PKG, "_calls.so")
+CALLS_FOR = os.path.join(BUILD, "calls.txt")  # what _calls.so was built with
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -72,24 +74,31 @@ def _compile(src: str, ptxas_verbose: bool, checks: bool = False) -> str:
 
 
 def build_calls() -> str:
-    src, header = os.path.join(CSRC, "calls.cpp"), os.path.join(ROOT, "include", "infllmv2.h")
-    if (os.path.exists(CALLS)
-            and os.path.getmtime(CALLS) >= max(os.path.getmtime(src), os.path.getmtime(header))):
-        return CALLS
     import torch
+    src, header = os.path.join(CSRC, "calls.cpp"), os.path.join(ROOT, "include", "infllmv2.h")
+    built_for = f"torch {torch.__version__}\npython {sys.version}\n"
+    if (os.path.exists(CALLS) and os.path.exists(CALLS_FOR)
+            and os.path.getmtime(CALLS) >= max(os.path.getmtime(src), os.path.getmtime(header))):
+        with open(CALLS_FOR) as f:
+            if f.read() == built_for:
+                return CALLS
     from torch.utils.cpp_extension import include_paths, library_paths
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     dirs = [os.path.join(ROOT, "include"), *include_paths(), sysconfig.get_path("include"),
             os.path.join(cuda, "include")]
-    tmp = CALLS + ".tmp"
+    tmp = f"{CALLS}.{os.getpid()}.o"  # (of its own: builds may run side by side)
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DINFLLMV2_TORCH="{torch.__version__}"',
            *(f"-I{d}" for d in dirs), src, "-o", tmp, *(f"-L{d}" for d in library_paths()),
            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stderr}")
     os.replace(tmp, CALLS)
+    os.makedirs(os.path.dirname(CALLS_FOR), exist_ok=True)
+    with open(CALLS_FOR, "w") as f:
+        f.write(built_for)
     return CALLS
 
 

@@ -271,4 +271,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
+// torch_version: the torch whose headers this was compiled with; its tensors'
+// layout is that version's alone.
+PyMODINIT_FUNC PyInit__calls() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", INFLLMV2_TORCH) != 0) Py_CLEAR(m);
+  return m;
+}

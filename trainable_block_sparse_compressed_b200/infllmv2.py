@@ -375,8 +375,11 @@ def _native():
     lib = load()
     if not os.path.exists(_CALLS_PATH):
         raise RuntimeError(f"call module not built: {_CALLS_PATH} (run __graft_entry__.build())")
-    import torch  # noqa: F401  (the module uses torch's libraries)
+    import torch  # (the module uses torch's libraries)
     from . import _calls as m
+    if m.torch_version != str(torch.__version__):
+        raise RuntimeError(f"call module built for torch {m.torch_version}, not {torch.__version__} "
+                           "(run __graft_entry__.build())")
     m.bind(*(ctypes.cast(getattr(lib, "infllmv2_" + f), ctypes.c_void_p).value
              for f in ("window_attn", "window_attn_backward", "paged_tables", "paged_append",
                        "paged_attn")))
