@@ -352,6 +352,11 @@ int infllmv2_window_attn(const infllmv2_params* p, int32_t window, int32_t n_sin
  *   contents need no preparation.  Calls that can run at the same time need a
  *   workspace each.
  * Sums have a fixed order: repeated calls give identical results.
+ * Scaled scores have to stay below 2^12 in magnitude (the forward's limit is far
+ * wider): P takes over the roundings of the fp32 lse and of its change of base,
+ * up to 5 * 2^-24 |lse| relative, which is below half a bf16 step (2^-9.7 against
+ * 2^-8) up to there and grows from there on; by 2^20 the gradients are off by
+ * tens of percent.
  */
 int infllmv2_window_attn_backward(const infllmv2_params* p, int32_t window, int32_t n_sink,
                                   const void* Q, const void* K, const void* V, const void* O,
