@@ -331,8 +331,11 @@ int infllmv2_prefill_varlen(const infllmv2_params* p, int32_t n_seqs,
  *   window >= 0, n_sink >= 0 (tokens; either may exceed T);
  *   Q [B, T, Hq, d], K, V [B, T, Hkv, d] bf16 (in); O [B, T, Hq, d] bf16, 32-byte
  *   aligned, lse [B, Hq, T] fp32 (out).
- * Keys and values must be finite: a value that is not can reach rows of its
- * 128-key tile that do not see it.  Scaled scores have to stay below 2^30 in
+ * All values must be finite, padding's and those that no row sees included: a
+ * weight of 0 meets every value of the 128-key tiles that a row's work item reads
+ * (up to two query tiles with the key tiles of both), so that one NaN or infinity
+ * can reach any row of its sequence and kv head, and no row of another.  Keys that
+ * a row does not see may hold anything.  Scaled scores have to stay below 2^30 in
  * magnitude (-inf counts as masked).
  */
 int infllmv2_window_attn(const infllmv2_params* p, int32_t window, int32_t n_sink, const void* Q,
@@ -352,6 +355,7 @@ int infllmv2_window_attn(const infllmv2_params* p, int32_t window, int32_t n_sin
  *   contents need no preparation.  Calls that can run at the same time need a
  *   workspace each.
  * Sums have a fixed order: repeated calls give identical results.
+ * All of Q, K, V, O and dO must be finite, unseen keys and padding included.
  * Scaled scores have to stay below 2^12 in magnitude (the forward's limit is far
  * wider): P takes over the roundings of the fp32 lse and of its change of base,
  * up to 5 * 2^-24 |lse| relative, which is below half a bf16 step (2^-9.7 against
@@ -453,10 +457,11 @@ int infllmv2_paged_append(const infllmv2_paged_params* p, const int32_t* slots, 
  *   time need a workspace each.
  * Only pages with a visible key are read: pages that left the window (and hold
  * no sink) may have been given to others.  Anything may lie in a sequence's
- * last page behind its last token.  An id outside the pool that is needed sets
- * INFLLMV2_STATUS_BAD_PAGE; its keys and values are read as zeros.  A row at a
- * position past the table (t >= max_pages * page_size: a token that found no
- * slot) gets O = 0 and lse = -inf; the sequence's other rows keep theirs.
+ * last page behind its last token; the values of its tokens must be finite (one
+ * that is not can reach any of the sequence's rows).  An id outside the pool that
+ * is needed sets INFLLMV2_STATUS_BAD_PAGE; its keys and values are read as zeros.
+ * A row at a position past the table (t >= max_pages * page_size: a token that
+ * found no slot) gets O = 0 and lse = -inf; the sequence's other rows keep theirs.
  * Negative lengths count as 0, lengths past 2^30 as 2^30, and rows past n_tokens
  * are cut.
  */

@@ -159,6 +159,30 @@ def test_window_attn_ignores_keys_outside(cuda_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,Hq,Hkv,window,at", [(600, 2, 2, 0, 200), (600, 2, 2, 2, 5), (4100, 32, 2, 100, 3000),
+                                                (1000, 16, 4, 64, 999)])
+def test_a_value_that_is_not_finite_stays_in_its_sequence_and_head(cuda_lib, T, Hq, Hkv, window, at):
+    """Rows that see it are NaN; which rows near it are is not promised, but
+    other sequences, other kv heads and all lse are untouched.  An unseen key
+    reaches no row at all."""
+    import torch
+    Q, K, V = make(3, T, Hq, Hkv, seed=T)
+    O, lse = run(cuda_lib, Q, K, V, window, 0)
+    V2 = V.clone()
+    V2[1, at, 0] = float("nan")
+    O2, lse2 = run(cuda_lib, Q, K, V2, window, 0)
+    G, last = Hq // Hkv, T if window == 0 else min(T, at + window)
+    assert torch.isnan(O2[1, at:last, :G]).all()
+    assert torch.equal(O2[0], O[0]) and torch.equal(O2[2], O[2]) and torch.equal(lse2, lse)
+    assert torch.equal(O2[1, :, G:], O[1, :, G:])
+    K2 = K.clone()
+    K2[1, T - 1, 0] = float("nan")      # seen by the last token alone
+    O3, lse3 = run(cuda_lib, Q, K2, V, window, 0)
+    assert torch.equal(O3[:, :T - 1], O[:, :T - 1]) and torch.equal(lse3[..., :T - 1], lse[..., :T - 1])
+    assert torch.isnan(O3[1, T - 1, :G]).all() and torch.isnan(lse3[1, :G, T - 1]).all()
+
+
+@pytest.mark.gpu
 def test_window_attn_side_stream_graph_and_repeat(cuda_lib):
     """On a side stream, captured and replayed on new inputs: the same bits."""
     import torch
