@@ -795,3 +795,71 @@ def test_prefill_varlen_against_the_oracle(cuda_lib):
                 o, l = orc.attend(Qf[t, hs], Kf[:, g], Vf[:, g], keys, op.sm_scale(128))
                 assert np.abs(Oi[r, hs] - o).max() <= O_ATOL
                 assert np.abs(Li[hs, r] - l).max() <= LSE_ATOL
+
+
+@pytest.mark.parametrize("op", ["dense", "sparse", "window", "window_backward", "paged", "decode"])
+def test_a_threads_first_cuda_call(cuda_lib, op):
+    """A new thread, which no CUDA call has bound to the device's context yet,
+    gets the main thread's results (operators that encode tensor maps)."""
+    import threading
+
+    import torch
+    api, T, Hq, Hkv = cuda_lib, 300, 16, 2
+    g = torch.Generator().manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    Q, K, V, dO = r(1, T, Hq, 128), r(1, T, Hkv, 128), r(1, T, Hkv, 128), r(1, T, Hq, 128)
+    p = api.make_params(1, T, Hq, Hkv, topk=8)
+    O, lse = torch.zeros_like(Q), torch.zeros(1, Hq, T, device="cuda")
+    out = [O, lse]
+    if op == "dense":
+        call = lambda s: api.dense_attn(p, Q, K, V, O, lse, stream=s)  # noqa: E731
+    elif op == "sparse":
+        idx = torch.arange(5, dtype=torch.int32).expand(1, Hkv, T, 5)
+        idx = torch.cat([idx, torch.full((1, Hkv, T, 3), -1, dtype=torch.int32)], -1).cuda()
+        ws = api.alloc_workspace(p, api.OP_ATTN)
+        call = lambda s: api.sparse_attn(p, Q, K, V, idx, O, lse, ws, stream=s)  # noqa: E731
+    elif op == "window":
+        call = lambda s: api.window_attn(p, 64, 4, Q, K, V, O, lse, stream=s)  # noqa: E731
+    elif op == "window_backward":
+        o, ls = torch.empty_like(Q), torch.empty_like(lse)
+        api.window_attn(p, 64, 4, Q, K, V, o, ls)
+        out, ws = [torch.zeros_like(x) for x in (Q, K, V)], api.alloc_workspace(p, api.OP_WINDOW_BACKWARD)
+        call = lambda s: api.window_attn_backward(p, 64, 4, Q, K, V, o, ls, dO, *out, ws, stream=s)  # noqa: E731
+    elif op == "paged":
+        pp = api.make_paged_params(1, 5, 5, 64, n_tokens=9, Hq=Hq, Hkv=Hkv)
+        pools, ws = (r(5, 64, Hkv, 128), r(5, 64, Hkv, 128)), api.alloc_paged_workspace(pp)
+        out = [torch.zeros(9, Hq, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(9, Hq, device="cuda")]
+        table, cu, lens = i32(4, 2, 0, 1, 3).view(1, 5), i32(0, 9), i32(T)
+        call = lambda s: api.paged_attn(pp, Q[0, :9], *pools, table, cu, lens, *out, ws, stream=s)  # noqa: E731
+    else:
+        Kc, ws = torch.zeros(1, api.num_compressed(T), Hkv, 2, 128, dtype=torch.bfloat16, device="cuda"), \
+            api.alloc_workspace(p, api.OP_DECODE)
+        api.compress_keys(p, K, Kc)
+        lens, k, v = i32(T - 1, 0, 0, 0), r(1, Hkv, 128), r(1, Hkv, 128)
+        out = [torch.zeros(1, Hq, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, Hq, device="cuda")]
+
+        def call(s):
+            api.decode_step(p, Q[:, 0].contiguous(), k, v, K, V, Kc, lens, *out, ws=ws, stream=s)
+            if s is None:           # (a thread's first CUDA call is the library's)
+                lens[0] = T - 1
+    call(None)
+    torch.cuda.synchronize()
+    want = [x.clone() for x in out]
+    for x in out:
+        x.zero_()
+    stream, errors = torch.cuda.current_stream(), []
+    torch.cuda.synchronize()
+
+    def work():
+        try:
+            call(stream)
+        except Exception as e:  # noqa: BLE001  (told to the main thread)
+            errors.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not errors and api.get_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(out, want))

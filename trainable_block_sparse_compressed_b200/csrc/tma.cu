@@ -36,10 +36,19 @@ int make_tmap_bf16_4d(CUtensorMap* map, const void* base, const uint64_t dims[4]
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return INFLLMV2_ERR_CUDA;
   const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
-                        strides_bytes, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto encode = [&] {
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+              strides_bytes, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r == CUDA_ERROR_INVALID_CONTEXT) {
+    // The runtime binds a thread to its device's context with the thread's first
+    // call that needs it, and this driver call may come before: bind it here.
+    int d = 0;
+    if (cudaGetDevice(&d) == cudaSuccess && cudaSetDevice(d) == cudaSuccess) r = encode();
+  }
   return r == CUDA_SUCCESS ? INFLLMV2_OK : INFLLMV2_ERR_CUDA;
 }
 
