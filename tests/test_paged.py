@@ -268,6 +268,32 @@ def test_paged_append(cuda_lib, n, Hkv, page, Hq):
     assert torch.equal(K, K2) and torch.equal(V, V2)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,Hkv,page", [(1, 1, 16), (3, 2, 64), (17, 3, 128), (1000, 8, 32), (4099, 2, 16)])
+@pytest.mark.parametrize("form", ["dense", "K dense", "V dense", "strided"])
+def test_paged_append_writes_untouched_pools(cuda_lib, n, Hkv, page, form):
+    """Pools that no call has written before: every slot's row arrives, densely
+    packed or strided, and nothing else changes."""
+    import torch
+    g = torch.Generator().manual_seed(n)
+    n_pages = -(-n // page) + 2
+    kv = torch.randn(n, 2 * Hkv + 1, 128, generator=g).to(torch.bfloat16).cuda()
+    k, v = kv[:, :Hkv], kv[:, Hkv + 1:]
+    if form in ("dense", "K dense"):
+        k = k.contiguous()
+    if form in ("dense", "V dense"):
+        v = v.contiguous()
+    K = torch.full((n_pages, page, Hkv, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    V = torch.full_like(K, 9.0)
+    slots = torch.randperm(n_pages * page, generator=g)[:n].cuda()
+    want = [x.flatten(0, 1).clone() for x in (K, V)]
+    want[0][slots], want[1][slots] = k, v
+    p = cuda_lib.make_paged_params(1, 1, n_pages, page, n_tokens=n, Hq=Hkv, Hkv=Hkv)
+    cuda_lib.paged_append(p, slots.to(torch.int32), k, v, K, V)
+    torch.cuda.synchronize()
+    assert torch.equal(K.flatten(0, 1), want[0]) and torch.equal(V.flatten(0, 1), want[1])
+
+
 # ---------------------------------------------------------------------------
 # attention over the cache
 # ---------------------------------------------------------------------------
@@ -384,6 +410,18 @@ def test_paged_attn_long_sequences_split(cuda_lib, window, n_sink):
 def test_paged_attn_chunks_under_short_windows(cuda_lib, window, n_sink, Hq, Hkv):
     b = Batch([(3000, 900), (700, 333), (20, 20), (5000, 1), (64, 0)], Hq, Hkv, 16, seed=4, pad=3)
     b.check(*b.run(cuda_lib, window, n_sink), window, n_sink, sample=150)
+
+
+@pytest.mark.gpu
+def test_paged_attn_sinks_without_a_window(cuda_lib):
+    """Every earlier key is visible anyway: the sinks change no bit."""
+    import torch
+    b = Batch([(900, 300), (640, 1), (77, 77)], 16, 4, 32, seed=13, pad=1)
+    want = b.run(cuda_lib, 0, 0)
+    for n_sink in (1, 130, 5000):
+        got = b.run(cuda_lib, 0, n_sink)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    b.check(*want)
 
 
 @pytest.mark.gpu
