@@ -413,7 +413,8 @@ typedef struct infllmv2_paged_params {
  * there gets slot -1 and sets the status again, until the caller enters a page
  * or gives kv_lens without those tokens.)  Tokens that outgrow max_pages get slot -1,
  * tokens past n_tokens get no row, and INFLLMV2_STATUS_SEQ_FULL is set.
- *   kv_lens, q_lens [n_seqs], free_pages [*free_count], free_count [1] int32 (in);
+ *   kv_lens, q_lens [n_seqs], free_pages [at least *free_count; not NULL even where
+ *   that is 0], free_count [1] int32 (in);
  *   block_table [n_seqs, max_pages] int32 (in/out); cu_q [n_seqs + 1],
  *   seqlens [n_seqs], slots, positions [n_tokens], free_left [1] int32 (out).
  * seqlens may be kv_lens and free_left may be free_count: then a captured call

@@ -79,6 +79,20 @@ def test_paged_tables_out_of_pages(cuda_lib):
 
 
 @pytest.mark.gpu
+def test_paged_tables_with_an_empty_free_list(cuda_lib):
+    """No page left and none needed, then one needed: an empty list is a list."""
+    api = cuda_lib
+    args = ([5, 30], [2, 2], [], [[0, -1], [2, 1]], 16, 4)
+    *ref, fine = wo.paged_tables(*args)
+    assert fine and run_tables(api, *args, 3) == tuple(ref)
+    assert api.get_status() == 0
+    args = ([16, 30], [2, 2], [], [[0, -1], [2, 1]], 16, 4)
+    *ref, fine = wo.paged_tables(*args)
+    assert not fine and run_tables(api, *args, 3) == tuple(ref)
+    assert api.get_status() == api.STATUS_NO_PAGE
+
+
+@pytest.mark.gpu
 def test_paged_tables_too_long_and_negative(cuda_lib):
     """A sequence that outgrows its table row, more tokens than rows, and
     lengths below zero: nothing is written outside, the status says so."""

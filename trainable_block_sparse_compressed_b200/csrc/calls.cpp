@@ -173,9 +173,11 @@ int paged_tables(PyObject* const* a) {
   const auto p = params<infllmv2_paged_params>(a[0]);
   const int64_t n = p.n_seqs, rows = p.n_tokens;
   const Device dev(a[6]);
+  const int64_t n_free = tensor(a[3]).numel();
   const int32_t *kv_lens = dev.i32(a[1], {n}), *q_lens = dev.i32(a[2], {n}),
-                *free_pages = dev.i32(a[3], {tensor(a[3]).numel()}),
-                *free_count = dev.i32(a[4], {1});
+                *free_pages = dev.i32(a[3], {n_free}), *free_count = dev.i32(a[4], {1});
+  // an empty tensor has no address; a list of no pages is not read
+  if (n_free == 0) free_pages = free_count;
   int32_t *table = dev.i32(a[5], {n, p.max_pages}), *cu_q = dev.i32(a[6], {n + 1}),
           *seqlens = dev.i32(a[7], {n}), *slots = dev.i32(a[8], {rows}),
           *positions = dev.i32(a[9], {rows}), *free_left = dev.i32(a[10], {1});

@@ -130,7 +130,7 @@ __device__ __forceinline__ SeqLens seq_lens(const FwdArgs& a, int i) {
   SeqLens s;
   const int r0 = __ldg(a.cu_q + i), r1 = __ldg(a.cu_q + i + 1);
   const int c0 = max(0, min(r0, a.n_tokens)), c1 = max(0, min(r1, a.n_tokens));
-  // (rows that are cut, at either end, leave the others their positions)
+  // (rows past n_tokens are cut, the others keep their positions)
   const long long len = min(max(static_cast<long long>(r1) - r0, 0ll), 1ll << 28);
   s.t0 = max(0, min(__ldg(a.seqlens + i), 1 << 30)) - static_cast<int>(len);
   s.row0 = c0;
