@@ -21,3 +21,17 @@ def test_checked_build_runs_clean(cuda_lib):
                        cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
     assert "smoke ok" in r.stdout
+
+
+def test_window_and_pages_run_clean_on_the_checked_build(cuda_lib):
+    """The tests of the windowed attention, its gradients and the paged cache
+    that assert an empty status, on the checked build."""
+    from trainable_block_sparse_compressed_b200 import build
+    lib = build.build(checks=True)
+    tests = [os.path.join(ROOT, "tests", f"test_{x}.py")
+             for x in ("paged", "window_attn", "window_attn_backward")]
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-m", "gpu", "-p", "no:cacheprovider", "-k",
+                        "all_elements or serving or split or short_windows or tables or past", *tests],
+                       cwd=ROOT, env=dict(os.environ, INFLLMV2_LIB=lib), capture_output=True, text=True,
+                       timeout=600)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-2000:]

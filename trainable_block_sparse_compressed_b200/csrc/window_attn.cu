@@ -813,7 +813,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int head = item.g * G + h;
         const int slot = 2 * blockIdx.x + (item.k0 > 0 ? 0 : 1);
         const int64_t prow = static_cast<int64_t>(slot) * kSlotRows + (item.pair ? w * 128 : 0) + r;
-        const bool write = row_ok && INFLLMV2_CHECK(ctx.status, !PAGED || (row >= 0 && row < a.n_tokens));
+        const bool write =
+            row_ok && INFLLMV2_CHECK(ctx.status, item.g < a.Hkv &&
+                                                     (PAGED ? row >= 0 && row < a.n_tokens
+                                                            : item.b < a.B && item.tok0 + my_tok < a.T));
         auto store = [&](const float (&v)[32], int c) {  // channels c .. c + 31
           uint32_t u[8];
           if (whole) {
@@ -935,11 +938,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 // added in order, so results repeat exactly.
 constexpr int kMergeThreads = 256, kMergeSplit = 16;
 
-__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const FwdArgs a, int G) {
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const FwdArgs a, int G,
+                                                                    int* status) {
   grid_wait();
   const int4 it = a.part_item[blockIdx.x];
   const int c = blockIdx.x, c0 = it.z;
   const int lane = lane_id();
+  if (!INFLLMV2_CHECK(status, it.y == 0 || (c0 >= 0 && c0 < c && it.y * G <= kSlotRows && it.x >= 0 &&
+                                            it.x + it.y <= a.n_tokens && it.w < a.Hkv)))
+    return;
   constexpr int kWarps = kMergeThreads / 32;
   for (int r = blockIdx.y * kWarps + warp_id(); r < it.y * G; r += kWarps * kMergeSplit) {
     auto prow = [&](int j) {
@@ -1084,7 +1091,7 @@ int launch_paged_attn(const infllmv2_paged_params& p, float scale_log2, const vo
   if (int e = rows_map(&tk, K_pages, p.n_pages, p.page_size, p.Hkv, ks, 1, p.page_size)) return e;
   if (int e = rows_map(&tv, V_pages, p.n_pages, p.page_size, p.Hkv, ks, 1, p.page_size)) return e;
   if (int e = launch<true>(G, tq, tk, tv, a, grid, ctx, st)) return e;
-  return launch_waiting(merge_kernel, dim3(grid, kMergeSplit), kMergeThreads, 0, st, a, G);
+  return launch_waiting(merge_kernel, dim3(grid, kMergeSplit), kMergeThreads, 0, st, a, G, ctx.status);
 }
 
 }  // namespace infllmv2

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(512, 2) stats_kernel(
     const __nv_bfloat16* __restrict__ V, const __nv_bfloat16* __restrict__ O,
     const __nv_bfloat16* __restrict__ dO, const float* __restrict__ lse,
     float* __restrict__ stats, int T, int Hkv, int n_qt, Visible vis, float scale_log2,
-    FewRows few) {
+    FewRows few, int n_bg, int* status) {
   grid_launch_next();
   constexpr int TPT = 128 / G;
   const int Hq = Hkv * G;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(512, 2) stats_kernel(
         pl += p;
       }
     }
-    if (sub == 0)
+    if (sub == 0 && INFLLMV2_CHECK(status, b * Hkv + g < n_bg && t < T))
       stats[((static_cast<int64_t>(b) * Hkv + g) * n_qt + t / TPT) * 256 + 128 + (t % TPT) * G + h % G] =
           pl == 0.f ? 0.f : pd / pl;
     return;
@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(512, 2) stats_kernel(
   const int tile = static_cast<int>(blockIdx.x - few_blocks);
   const int bg = tile / n_qt, qt = tile % n_qt;
   const int b = bg / Hkv, g = bg % Hkv;
+  if (!INFLLMV2_CHECK(status, bg < n_bg)) return;
   float* out = stats + static_cast<int64_t>(tile) * 256;
   uint4 o[4], g4[4];
   float l2[4];
@@ -573,6 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t acc = (w ? tdK : tdV) + lane_addr;
       __nv_bfloat16* out = (w ? a.dK : a.dV) +
                            ((static_cast<int64_t>(it.b) * a.T + key) * a.Hkv + it.g) * kHeadDim;
+      const bool store = INFLLMV2_CHECK(ctx.status, it.bg < a.B * a.Hkv && it.kt < a.n_kt &&
+                                                        it.q0 >= 0 && it.q1 < a.n_qt);
       const int slot = 2 * blockIdx.x + (it.begins ? 1 : 0);
       float* part = a.part + ((static_cast<int64_t>(slot) * 2 + w) * 128 + key_r) * kHeadDim;
 #pragma unroll 1
@@ -581,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(acc + c, v);
         tmem_ld_wait();
         uint32_t u[8];
+        if (!store) continue;
         if (!whole) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -600,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.acc_free);
-      if (threadIdx.x == kThreads - 1 && !it.begins && it.ends)
+      if (threadIdx.x == kThreads - 1 && !it.begins && it.ends && store)
         a.part_item[blockIdx.x] =
             make_int4(it.bg, it.kt, static_cast<int>((a.per * blockIdx.x - it.off) / a.per), 1);
     }
@@ -617,11 +621,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // left its piece in slot 2 c0 + 1, the others in slot 2 j), in order.  Blocks
 // (c, part of the 2 x 128 x 128 values).
 constexpr int kMergeSplit = 32;
-__global__ void __launch_bounds__(256) dkv_merge_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(256) dkv_merge_kernel(const BwdArgs a, int* status) {
   grid_wait();
   const int4 it = a.part_item[blockIdx.x];
   if (it.w == 0) return;
   const int c = blockIdx.x, c0 = it.z;
+  if (!INFLLMV2_CHECK(status, c0 >= 0 && c0 < c && it.x < a.B * a.Hkv)) return;
   constexpr int kN = 2 * 128 * 32 / kMergeSplit;  // float4 per block
   for (int i = blockIdx.y * kN + threadIdx.x; i < (blockIdx.y + 1) * kN; i += blockDim.x) {
     const int w = i >> 12, r = (i >> 5) & 127, ch = (i & 31) * 4;
@@ -904,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[16];
         tmem_ld16(tdQ + lane_addr + 64 * w + c, v);
         tmem_ld_wait();
-        if (t < a.T) {
+        if (t < a.T && INFLLMV2_CHECK(ctx.status, it.qt >= 0 && it.b < a.B)) {
           uint32_t u[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -970,7 +975,7 @@ int launch_g(const void* Q, const void* K, const void* V, const void* O, const f
       static_cast<const __nv_bfloat16*>(Q), static_cast<const __nv_bfloat16*>(K),
       static_cast<const __nv_bfloat16*>(V), static_cast<const __nv_bfloat16*>(O),
       static_cast<const __nv_bfloat16*>(dO), lse, const_cast<float*>(a.stats), a.T, a.Hkv, a.n_qt,
-      a.vis, a.scale_log2, few);
+      a.vis, a.scale_log2, few, a.B * a.Hkv, ctx.status);
   static std::atomic<uint64_t> kv_set{0}, q_set{0};
   if (int e = set_smem_limit(dkv_kernel<G>, kDkvSmem, kv_set)) return e;
   if (int e = set_smem_limit(dq_kernel<G>, kDqSmem, q_set)) return e;
@@ -981,7 +986,7 @@ int launch_g(const void* Q, const void* K, const void* V, const void* O, const f
   const unsigned q_ctas = static_cast<unsigned>(items < sms ? items : sms);
   if (int e = launch_waiting(dq_kernel<G>, q_ctas, kThreads, kDqSmem, st, tq, tdo, tk, tv, a, ctx))
     return e;
-  return launch_waiting(dkv_merge_kernel, dim3(ctas, kMergeSplit), 256, 0, st, a);
+  return launch_waiting(dkv_merge_kernel, dim3(ctas, kMergeSplit), 256, 0, st, a, ctx.status);
 }
 
 // [B, T, heads, 128] bf16, boxes of 64 channels x box_heads x box_rows.
