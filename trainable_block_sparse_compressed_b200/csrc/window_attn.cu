@@ -440,34 +440,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       // paged: lane l takes the l-th page of a tile, its id loaded a tile ahead
       const int ppt = PAGED ? kKeyTile / a.page : 1;
       const int32_t* row = PAGED ? a.table + static_cast<int64_t>(item.b) * a.max_pages : nullptr;
-      constexpr int kNoKey = -2;  // no visible key in the page: it is not loaded
-      auto page_id = [&](int i) -> int {
-        if (i >= item.k1 || lane >= ppt) return kNoKey;
+      auto needs = [&](int i) -> bool {  // the page has a visible key
         const int col = item.kt.tile(i) * ppt + lane;
         const int c0 = col * a.page;
-        const bool need = c0 <= t_last && (c0 + a.page > w_begin || c0 < a.vis.n_sink);
-        if (!need || col >= a.max_pages) return kNoKey;
-        // any id outside the pool counts as -1: a page in front of the tensor,
-        // of which the copies read zeros
-        const int id = __ldg(row + col);
-        return id >= 0 && id < a.n_pages ? id : -1;
+        return i < item.k1 && lane < ppt && col < a.max_pages && c0 <= t_last &&
+               (c0 + a.page > w_begin || c0 < a.vis.n_sink);
       };
-      int next_id = PAGED ? page_id(item.k0) : 0;
+      auto page_id = [&](int i, bool needed) -> int {
+        return needed ? __ldg(row + item.kt.tile(i) * ppt + lane) : 0;
+      };
+      bool next_need = PAGED && needs(item.k0);
+      int next_id = PAGED ? page_id(item.k0, next_need) : 0;
       for (int i = item.k0; i < item.k1; ++i, ++n) {
         const int id = next_id;
-        if (PAGED) next_id = page_id(i + 1);
+        const bool need = next_need;
+        if (PAGED) next_need = needs(i + 1), next_id = page_id(i + 1, next_need);
         if (n >= stages && !(ok = warp_wait(&empty[st], ph ^ 1, ctx, abort_flag))) break;
         uint8_t* dst = ring + st * kTileBytes;
         if (PAGED) {
-          const bool need = id != kNoKey;
           const uint32_t box = static_cast<uint32_t>(a.page) * 128;
           const uint32_t cnt = __popc(__ballot_sync(0xffffffffu, need));
           if (lane == 0) mbar_arrive_expect_tx(&full[st], cnt * 2 * box);
           __syncwarp();
           if (need) {
-            if (id < 0) report_status(ctx.status, INFLLMV2_STATUS_BAD_PAGE);
+            // any id outside the pool counts as -1: a page in front of the tensor,
+            // of which the copies read zeros
+            const bool bad = id < 0 || id >= a.n_pages;
+            if (bad) report_status(ctx.status, INFLLMV2_STATUS_BAD_PAGE);
             for (int h = 0; h < 2; ++h)
-              tma_load_4d(dst + h * 16384 + lane * box, tm, &full[st], 64 * h, item.g, 0, id);
+              tma_load_4d(dst + h * 16384 + lane * box, tm, &full[st], 64 * h, item.g, 0,
+                          bad ? -1 : id);
           }
         } else if (lane == 0) {
           mbar_arrive_expect_tx(&full[st], kTileBytes);
