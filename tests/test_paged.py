@@ -662,6 +662,63 @@ def test_serving_loop(cuda_lib, window, n_sink, page):
               total[i])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,n_sink,page", [(0, 0, 64), (20, 3, 16)])
+def test_decode_step_captured_and_replayed(cuda_lib, window, n_sink, page):
+    """Tables, append and attention of a decode step as one graph, lengths and
+    the free count in place: 70 replays with new rows, every row against the
+    oracle over the whole sequences."""
+    import torch
+    api = cuda_lib
+    Hq, Hkv, steps, start = 8, 2, 70, [0, 5, 63, 16, 40]
+    n, width = len(start), -(-(max(start) + steps) // page)
+    g = torch.Generator().manual_seed(17)
+    pages = [-(-x // page) for x in start]
+    n_pages = sum(-(-(x + steps) // page) for x in start)
+    perm = torch.randperm(n_pages, generator=g).tolist()
+    table, at = [], 0
+    for h in pages:
+        table.append(perm[at:at + h] + [-1] * (width - h))
+        at += h
+    free = perm[at:]
+    old = [torch.randn(x, 2 * Hkv, 128, generator=g).to(torch.bfloat16) for x in start]
+    new = torch.randn(steps, n, Hq + 2 * Hkv, 128, generator=g).to(torch.bfloat16)
+    K = torch.full((n_pages, page, Hkv, 128), float("nan"), dtype=torch.bfloat16)
+    V = K.clone()
+    for i, x in enumerate(old):
+        for t in range(start[i]):
+            K[table[i][t // page], t % page] = x[t, :Hkv]
+            V[table[i][t // page], t % page] = x[t, Hkv:]
+    K, V, lens, count = K.cuda(), V.cuda(), i32(start), i32([len(free)])
+    tab, fr, q = i32(table), i32(free), i32([1] * n)
+    cu, slots, pos = i32([0] * (n + 1)), i32([0] * n), i32([0] * n)
+    x, O = new[0].cuda(), torch.zeros(n, Hq, 128, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(n, Hq, device="cuda")
+    p = api.make_paged_params(n, width, n_pages, page, n_tokens=n, Hq=Hq, Hkv=Hkv, window=window,
+                              n_sink=n_sink)
+    ws = api.alloc_paged_workspace(p)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            api.paged_tables(p, lens, q, fr, count, tab, cu, lens, slots, pos, count)
+            api.paged_append(p, slots, x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], K, V)
+            api.paged_attn(p, x[:, :Hq], K, V, tab, cu, lens, O, lse, ws)
+    got = []
+    for step in range(steps):
+        x.copy_(new[step])
+        graph.replay()
+        got.append((f64(O), f64(lse)))
+    torch.cuda.synchronize()
+    assert api.get_status() == 0 and count.item() == 0 and lens.tolist() == [s + steps for s in start]
+    a = f64(new)
+    for i in range(n):
+        kv = np.concatenate([f64(old[i]), a[:, i, Hq:]])
+        ref = wo.attention(a[:, i, :Hq], kv[:, :Hkv], kv[:, Hkv:], start[i] + np.arange(steps), window,
+                           n_sink)
+        check(np.stack([o[i] for o, _ in got]), np.stack([ls[i] for _, ls in got]), ref, start[i] + steps)
+
+
 # ---------------------------------------------------------------------------
 # refusals (no GPU needed)
 # ---------------------------------------------------------------------------
