@@ -1,9 +1,10 @@
 // paged.cu -- the paged key/value cache: block tables and slot maps built on
 // the GPU from the requests' lengths, and the append of new keys and values.
 //
-// Measured on one B200, replayed in a graph: tables of 16 requests 3.2-4.5 us, of
-// 1024 requests with 45000 new tokens 9 us; append of 16 tokens 1.8 us, of 8192
-// tokens of 8 kv heads (67 MB) 12 us from HBM (5.5 TB/s).
+// Measured on one B200, replayed in a graph: tables of 16 requests 4.6 us, of
+// 1024 requests with 44000 new tokens 9 us; append of 16 tokens 1.8 us, of 8192
+// tokens of 8 kv heads (67 MB) 12.4 us from HBM (5.4 TB/s).  Calls in a row from
+// Python: 6.2, 10.3, 4 and 14.4 us.
 //
 // Tables.  For request i with kv_i cached and q_i new tokens, pages of P:
 //   have_i = ceil(kv_i / P), want_i = ceil((kv_i + q_i) / P), neither more than max_pages,

@@ -69,9 +69,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const 
 }
 
 // Likewise, with a vote at every poll instead of one behind them: the loop keeps
-// the warp's values in uniform registers.  For the issuers of long contiguous
-// items (T=32768, window 4096: 2013 us, with warp_wait 2050); single tokens and
-// short chunks over pages are 1 % faster with warp_wait.
+// the warp's values in uniform registers.  For the issuers of contiguous items
+// (T=32768, window 4096: 2013 us, with warp_wait 2050); mixed chunks over pages
+// take warp_wait (48.5 us, with warp_poll 49.0).
 __device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, const DevCtx& ctx,
                                           volatile int* abort_flag) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;

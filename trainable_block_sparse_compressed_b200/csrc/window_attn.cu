@@ -36,10 +36,10 @@
 // on the exponentials of 64 keys (512 on the special-function unit alone, which
 // two warps of a scheduler share) and ~700 on loads, stores and barriers; the
 // tensor core's four products are done in ~2500 of the ~3500 cycles of a tile.
-// In a long run the power cap lowers the clock to ~1.4 GHz.  One B200, T=32768,
-// 32 heads, window 4096, 64 sinks: 1.87 ms (1.12 PFLOP/s) in a short run, 2.03 ms
-// in a long one.  Single tokens are bound by HBM: 16 x 131072 tokens, 2.15 GB:
-// 330 us (6.5 TB/s) short, 358 us long.
+// In a long run the power cap lowers the clock to ~1.4 GHz.  One B200, calls in a
+// row: T=32768, 32 heads, window 4096, 64 sinks 2.0-2.1 ms (1.0 PFLOP/s).  Single
+// tokens are bound by HBM: 16 x 131072 tokens, 2.15 GB, 340-370 us from card to
+// card (5.8-6.3 TB/s).
 // Tried and slower: S in one 128-wide product per tile (P V, S and the softmax
 // of a stream then wait for each other, 4350 cycles; with the streams taking
 // turns at the exponentials), two softmax warpgroups per stream (a barrier per
